@@ -25,6 +25,14 @@ constexpr int kMaxWorkGroups = 2048;
 // walk that leaves the window reads global memory.
 constexpr int kWindowBefore = 768;
 
+// a + b for a, b >= 0, held at 2^31 - 1.  Lengths are whatever the device
+// holds, and a sum of tokens that wrapped would place a token before the
+// first one of its request.  Held sums do not depend on their order.
+__device__ __forceinline__ int held_sum(int a, int b) {
+  return static_cast<int>(min(static_cast<uint32_t>(a) + static_cast<uint32_t>(b),
+                              static_cast<uint32_t>(kInt32Max)));
+}
+
 // Index of the last request whose prefix is <= x, for 0 <= x below the sum.
 __device__ __forceinline__ int find_request(const int32_t* prefix, int B, int x) {
   int lo = 0, hi = B;
@@ -94,10 +102,10 @@ __global__ __launch_bounds__(kThreads) void layout_kernel(LayoutArgs a) {
   int my_tokens = 0, my_blocks = 0, my_lack = 0, my_longest = 0;
   Request kept[PER ? PER : 1];
   auto sum_up = [&](const Request& r) {
-    my_tokens += r.added;
-    my_blocks += r.fit;
-    my_lack += r.lack;
-    my_longest = max(my_longest, r.cached + r.added);
+    my_tokens = held_sum(my_tokens, r.added);
+    my_blocks += r.fit;   // at most the entries of the table
+    my_lack = held_sum(my_lack, r.lack);
+    my_longest = max(my_longest, held_sum(r.cached, r.added));
   };
   if constexpr (PER) {
 #pragma unroll
@@ -115,7 +123,7 @@ __global__ __launch_bounds__(kThreads) void layout_kernel(LayoutArgs a) {
   for (int d = 1; d < 64; d <<= 1) {
     const int ut = __shfl_up(st, d), ub = __shfl_up(sb, d);
     if (lane >= d) {
-      st += ut;
+      st = held_sum(st, ut);
       sb += ub;
     }
   }
@@ -123,7 +131,7 @@ __global__ __launch_bounds__(kThreads) void layout_kernel(LayoutArgs a) {
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       my_longest = max(my_longest, __shfl_xor(my_longest, d));
-      my_lack += __shfl_xor(my_lack, d);
+      my_lack = held_sum(my_lack, __shfl_xor(my_lack, d));
     }
   }
   if (lane == 63) {
@@ -132,13 +140,14 @@ __global__ __launch_bounds__(kThreads) void layout_kernel(LayoutArgs a) {
     sums[2][wave] = my_longest;
     sums[3][wave] = my_lack;
   }
+  const int lane_before = __shfl_up(st, 1);   // a held sum cannot be taken back from
   __syncthreads();
-  int tokens = 0, blocks = 0, pt = st - my_tokens, pb = sb - my_blocks;
+  int tokens = 0, blocks = 0, pt = lane ? lane_before : 0, pb = sb - my_blocks;
 #pragma unroll
   for (int w = 0; w < kThreads / 64; ++w) {
-    pt += w < wave ? sums[0][w] : 0;
+    pt = held_sum(pt, w < wave ? sums[0][w] : 0);
     pb += w < wave ? sums[1][w] : 0;
-    tokens += sums[0][w];
+    tokens = held_sum(tokens, sums[0][w]);
     blocks += sums[1][w];
   }
   const int avail = max(0, a.num_free - first);
@@ -149,7 +158,7 @@ __global__ __launch_bounds__(kThreads) void layout_kernel(LayoutArgs a) {
       cached_of[b] = r.cached;
       held_of[b] = r.held;
     }
-    pt += r.added;
+    pt = held_sum(pt, r.added);
     pb += r.fit;
   };
   if constexpr (PER) {
@@ -175,11 +184,11 @@ __global__ __launch_bounds__(kThreads) void layout_kernel(LayoutArgs a) {
 #pragma unroll
       for (int w = 0; w < kThreads / 64; ++w) {
         longest = max(longest, sums[2][w]);
-        lacking += sums[3][w];
+        lacking = held_sum(lacking, sums[3][w]);
       }
       a.q_start[a.B] = tokens;
       a.status[0] = first + taken;
-      a.status[1] = lacking + blocks - taken;
+      a.status[1] = held_sum(lacking, blocks - taken);
       a.status[2] = tokens;
       a.status[3] = longest;
     }
@@ -188,9 +197,10 @@ __global__ __launch_bounds__(kThreads) void layout_kernel(LayoutArgs a) {
   auto cached = [&](int b) { return PER ? cached_of[b] : max(0, a.cached_lens[b]); };
   auto held = [&](int b) { return PER ? held_of[b] : max(0, a.blocks_held[b]); };
   const int stride = gridDim.x * kThreads;
-  for (int j = blockIdx.x * kThreads + tid; j < blocks; j += stride) {
+  for (uint32_t x = blockIdx.x * kThreads + tid; x < static_cast<uint32_t>(blocks); x += stride) {
+    const int j = static_cast<int>(x);
     const int b = find_request(first_block, a.B, j);
-    const int e = held(b) + j - first_block[b];
+    const int e = held(b) + (j - first_block[b]);
     a.block_table[static_cast<int64_t>(b) * a.table_width + e] =
         j < avail ? a.free_blocks[first + j] : -1;
   }
@@ -205,12 +215,13 @@ __global__ __launch_bounds__(kThreads) void layout_kernel(LayoutArgs a) {
     }
     if (t0 + tid >= a.T) continue;
     const int t = static_cast<int>(t0) + tid;
-    int b = -1, i = 0, slot = -1, position = 0;
+    int b = -1, i = 0, c = 0, slot = -1, depth = 0;
     if (t < tokens) {
       b = find_request(first_token, a.B, t);
       i = t - first_token[b];
+      c = cached(b);
       const int h = held(b);
-      const uint32_t at = static_cast<uint32_t>(cached(b)) + static_cast<uint32_t>(i);
+      const uint32_t at = static_cast<uint32_t>(c) + static_cast<uint32_t>(i);
       const uint32_t e = at / static_cast<uint32_t>(a.block_size);
       int page = -1;
       if (e < static_cast<uint32_t>(a.table_width)) {
@@ -224,7 +235,7 @@ __global__ __launch_bounds__(kThreads) void layout_kernel(LayoutArgs a) {
       }
       if (page >= 0 && page < a.num_blocks)
         slot = page * a.block_size + static_cast<int>(at - e * static_cast<uint32_t>(a.block_size));
-      position = static_cast<int>(at);
+      depth = i;
     }
     uint64_t* mask = a.tree_mask ? a.tree_mask + static_cast<int64_t>(t) * a.mask_words : nullptr;
     if (b < 0) {
@@ -233,7 +244,8 @@ __global__ __launch_bounds__(kThreads) void layout_kernel(LayoutArgs a) {
       // From the token to its root; indices fall, so the walk ends and each
       // mask word is complete when the walk has left it.
       const int base = t - i;
-      int depth = 0, word = mask ? a.mask_words : 0;
+      int word = mask ? a.mask_words : 0;
+      depth = 0;
       uint64_t bits = 0;
       for (int at = i;;) {
         if (mask) {
@@ -256,7 +268,6 @@ __global__ __launch_bounds__(kThreads) void layout_kernel(LayoutArgs a) {
         bits = 0;
         --word;
       }
-      position += depth - i;
     } else if (mask) {
       for (int w = 0; w < a.mask_words; ++w) {
         const int left = i + 1 - 64 * w;
@@ -264,7 +275,7 @@ __global__ __launch_bounds__(kThreads) void layout_kernel(LayoutArgs a) {
       }
     }
     a.slots[t] = slot;
-    a.positions[t] = position;
+    a.positions[t] = held_sum(c, depth);
     a.requests[t] = b;
   }
 }

@@ -375,6 +375,7 @@ typedef struct awq_kv_cache {
  *                       but not gained, tokens, longest c + n}
  * parents (T, NULL: chains): index in its request of the token that token i
  * follows; an index outside [0, i) makes it a root (depth 0).
+ * Sums, positions and lengths past 2^31 - 1 are held there.
  * T is the capacity of the token arrays: tokens past it are not written,
  * rows past the batch's tokens get slot -1, position 0, request -1 and an
  * empty mask.  The outputs must not overlap the inputs (block_table is

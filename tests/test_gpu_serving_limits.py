@@ -1,0 +1,95 @@
+"""Serving-pass operators on the GPU where lengths, scores and values reach
+the ends of their types, and in kernel variants that need many keys."""
+import sys
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import bit_weight_quantized_awq_amd as awq  # noqa: E402
+
+DEV = "cuda:0"
+MOST = 2 ** 31 - 1
+
+
+def say(msg):
+    print(f"\n[case] {msg}", flush=True)
+    sys.stdout.flush()
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    awq.lib()
+    yield
+
+
+def i32(x):
+    return torch.as_tensor(np.asarray(x), dtype=torch.int32).to(DEV)
+
+
+def num(t):
+    return t.detach().cpu().numpy()
+
+
+# ------------------------------------------------------------------------------- batch_layout
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("B,large", [(4, [0, 1]), (5, [0, 1, 2, 3, 4]), (300, list(range(20, 300))),
+                                     (700, [300, 301, 302]), (1500, [3, 700, 1400, 1401])])
+def test_layout_sums_past_32_bits(B, large, tree):
+    """Token counts whose sums pass 2^31: held there, and every token that
+    there is room for is placed as in 64 bits."""
+    say(f"batch_layout sums past 32 bits B={B} tree={tree}")
+    T, W, bs, F = 600, 2, 16, 40
+    cached = np.full(B, 9, dtype=np.int64)
+    counts = 1 + np.arange(B, dtype=np.int64) % 3
+    counts[large] = MOST - np.arange(len(large))
+    held = np.ones(B, dtype=np.int64)
+    start = np.concatenate([[0], np.cumsum(counts)])
+    table = np.full((B, W), -1, dtype=np.int32)
+    table[:, 0] = 100 + np.arange(B)
+    parents = np.array([-1 if t % 5 == 0 else 0 for t in range(T)], dtype=np.int32)
+    dev = i32(table)
+    got = awq.batch_layout(i32(cached), i32(counts), i32(held), i32(np.arange(F)), dev, bs, 2000, T,
+                           parents=i32(parents) if tree else None, mask_words=1)
+    np.testing.assert_array_equal(num(got.q_start), np.minimum(start, MOST))
+    need = -(-(cached + counts) // bs) - held
+    fit = np.minimum(need, W - 1)
+    gained = np.minimum(np.maximum(F - (np.cumsum(fit) - fit), 0), fit)
+    np.testing.assert_array_equal(num(got.blocks_held), held + gained)
+    np.testing.assert_array_equal(num(got.status), np.minimum(
+        [gained.sum(), (need - gained).sum(), start[-1], (cached + counts).max()], MOST))
+    table[:, 1] = np.where(gained > 0, np.cumsum(gained) - 1, -1)
+    np.testing.assert_array_equal(num(dev), table)
+    t = np.arange(T)
+    b = np.searchsorted(start, t, side="right") - 1
+    inside = t < start[-1]
+    b = np.where(inside, b, 0)
+    i = t - start[b]
+    first = parents if tree else i - 1
+    # Here a parent is none or the request's token 0, itself a root.
+    depth = np.where((first >= 0) & (first < i), 1, 0) if tree else i
+    at = cached[b] + i
+    page = np.where(at // bs < W, table[b, np.minimum(at // bs, W - 1)], -1)
+    np.testing.assert_array_equal(num(got.requests), np.where(inside, b, -1))
+    np.testing.assert_array_equal(num(got.positions), np.where(inside, cached[b] + depth, 0))
+    np.testing.assert_array_equal(num(got.slots),
+                                  np.where(inside & (page >= 0), page * bs + at % bs, -1))
+    for x in np.flatnonzero(inside):
+        want = {int(i[x])} if tree else set(range(int(i[x]) + 1))
+        if tree and depth[x]:
+            want.add(0)
+        bits = int(num(got.tree_mask)[x, 0]) & (2 ** 64 - 1)
+        assert bits == sum(1 << w for w in want if w < 64), x
+
+
+def test_layout_positions_past_32_bits():
+    say("batch_layout positions past 32 bits")
+    got = awq.batch_layout(i32([MOST - 1, MOST]), i32([4, 2]), i32([MOST, 0]), i32([0]),
+                           i32([[5], [6]]), 16, 8, 6)
+    np.testing.assert_array_equal(num(got.positions), [MOST - 1] + [MOST] * 5)
+    np.testing.assert_array_equal(num(got.slots), [-1] * 6)
+    assert num(got.status)[3] == MOST
