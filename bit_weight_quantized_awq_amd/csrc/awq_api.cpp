@@ -5,10 +5,12 @@
 
 #include "awq.h"
 #include "awq_device.h"
+#include "awq_lock.h"
 #include "awq_plan.h"
 
 using awq::Plan;
 using awq::Problem;
+using awq::WorkspaceLock;
 
 extern "C" {
 
@@ -98,6 +100,7 @@ int run_gemm(const Problem& p, const void* x, const void* qweight, const void* q
     if (!workspace || workspace_bytes < pl.ws_bytes) return AWQ_ERROR_WORKSPACE;
     if (!awq::aligned(workspace, 16)) return AWQ_ERROR_MISALIGNED;
   }
+  const WorkspaceLock lock(pl.ws_bytes > 0 || perm ? workspace : nullptr);
   const bool fused_gather = perm && pl.path == AWQ_PATH_DECODE && pl.decode_lds &&
                             pl.steps <= 4 && p.M <= awq::decode_gather_max_m();
   if (perm && !fused_gather) {

@@ -4,6 +4,7 @@
 
 #include "awq.h"
 #include "awq_device.h"
+#include "awq_lock.h"
 #include "awq_plan.h"
 #include "awq_verify.h"
 
@@ -104,6 +105,7 @@ int awq_tree_attention(const void* q, const awq_kv_cache* cache, const void* blo
     if (!workspace || workspace_bytes < need) return AWQ_ERROR_WORKSPACE;
     if (!awq::aligned(workspace, 256)) return AWQ_ERROR_MISALIGNED;
   }
+  const awq::WorkspaceLock lock(workspace);
   return status_of(awq::launch_attention(a, workspace, static_cast<hipStream_t>(stream)));
 }
 

@@ -260,21 +260,23 @@ PyObject* kv_write(PyObject*, PyObject* const* args, Py_ssize_t count) {
 
 // Workspaces by device and stream, from the function that serving.py sets (the
 // one that awq_gemm's come from).  A buffer that it has replaced by a larger
-// one stays allocated, so one held here stays valid.
+// one stays allocated, so one held here stays valid.  While that function
+// runs, another thread may come here for the same stream: each takes the
+// buffer that it was given.
 PyObject* workspace_source = nullptr;
-const Tensor& workspace_for(at::Device device, void* stream, size_t bytes) {
+Tensor workspace_for(at::Device device, void* stream, size_t bytes) {
   static auto* held = new std::map<std::pair<int, void*>, Tensor>;   // lives as long as the process
   Tensor& t = (*held)[{device.index(), stream}];
-  if (!t.defined() || static_cast<size_t>(t.numel()) < bytes) {
-    if (!workspace_source) throw Refused{PyExc_RuntimeError, "no source of workspaces"};
-    PyObject* o = PyObject_CallFunction(workspace_source, "iKK", static_cast<int>(device.index()),
-                                        static_cast<unsigned long long>(reinterpret_cast<uintptr_t>(stream)),
-                                        static_cast<unsigned long long>(bytes));
-    if (!o) throw PythonError{};
-    t = tensor("workspace", o);
-    Py_DECREF(o);
-  }
-  return t;
+  if (t.defined() && static_cast<size_t>(t.numel()) >= bytes) return t;
+  if (!workspace_source) throw Refused{PyExc_RuntimeError, "no source of workspaces"};
+  PyObject* o = PyObject_CallFunction(workspace_source, "iKK", static_cast<int>(device.index()),
+                                      static_cast<unsigned long long>(reinterpret_cast<uintptr_t>(stream)),
+                                      static_cast<unsigned long long>(bytes));
+  if (!o) throw PythonError{};
+  const Tensor given = tensor("workspace", o);
+  Py_DECREF(o);
+  t = given;
+  return given;
 }
 PyObject* set_workspace_source(PyObject*, PyObject* f) {
   Py_INCREF(f);
@@ -329,14 +331,16 @@ PyObject* tree_attention(PyObject*, PyObject* const* args, Py_ssize_t count) {
     }
     void* stream = stream_of(device);
     const size_t bytes = awq_tree_attention_workspace_size(B, T, heads, cache.heads, dim);
-    if (!ws && bytes) ws = &workspace_for(device, stream, bytes);
+    const Tensor own = !ws && bytes ? workspace_for(device, stream, bytes) : Tensor();
+    if (own.defined()) ws = &own;
+    void* const ws_data = ws ? ws->data_ptr() : nullptr;
+    const size_t ws_bytes = ws ? ws->nbytes() : 0;
     const Tensor out = given ? *given : new_tensor({T, heads, dim}, q.scalar_type(), device);
     const int st = unlocked([&] {
       return awq_tree_attention(T ? q.data_ptr() : nullptr, &cache, table.data_ptr(),
                                 cached.data_ptr(), q_start.data_ptr(), pointer(mask),
                                 T ? out.data_ptr() : nullptr, B, T, heads, W, table.stride(0), words,
-                                qs[0], qs[1], scale, dtype, ws ? ws->data_ptr() : nullptr,
-                                ws ? ws->nbytes() : 0, stream);
+                                qs[0], qs[1], scale, dtype, ws_data, ws_bytes, stream);
     });
     if (st != AWQ_SUCCESS) return status(st);
     if (given) {

@@ -138,8 +138,10 @@ int awq_gemm_plan(int64_t M, int64_t K, int64_t N, int64_t group_size,
  * workspace: device memory of at least awq_gemm_workspace_size(...) bytes, or
  * NULL when that is 0.  It must be zero-filled once before its first use; the
  * kernels leave it re-usable (all counters back at zero) on exit, so the same
- * buffer serves later calls on the same stream.  Two calls that may run
- * concurrently (different streams) must not share a workspace.  A HIP graph
+ * buffer serves later calls on the same stream, also from several host
+ * threads (a call's launches are not interleaved with those of another call
+ * with the same workspace pointer).  Two calls that may run concurrently
+ * (different streams) must not share a workspace.  A HIP graph
  * that captured a call keeps its workspace pointer: the buffer must stay
  * allocated (and unused by anything else) for as long as the graph may be
  * replayed.  A split prefill call, and a split decode call of more than

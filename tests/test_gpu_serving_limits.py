@@ -93,3 +93,51 @@ def test_layout_positions_past_32_bits():
     np.testing.assert_array_equal(num(got.positions), [MOST - 1] + [MOST] * 5)
     np.testing.assert_array_equal(num(got.slots), [-1] * 6)
     assert num(got.status)[3] == MOST
+
+
+# ------------------------------------------------------------------------------- host threads
+def test_host_threads_on_one_stream():
+    """Attention split over work-groups and products split along K from four
+    host threads on one stream, through one workspace: the same bits as from
+    one thread."""
+    import threading
+
+    import awq_inputs
+    say("host threads on one stream")
+    gen = torch.Generator(DEV).manual_seed(0)
+
+    def rand(*shape):
+        return torch.randn(shape, generator=gen, device=DEV).to(torch.float16)
+
+    def attention(ctx, n, heads, kvh):
+        blocks = -(-(ctx + n) // 16)
+        kc, vc, q = rand(blocks, 16, kvh, 128), rand(blocks, 16, kvh, 128), rand(n, heads, 128)
+        table, cached, start = i32([list(range(blocks))]), i32([ctx]), i32([0, n])
+        return lambda: awq.tree_attention(q, kc, vc, table, cached, start)
+
+    def product(M, K, N):
+        p = awq_inputs.make_inputs(M, K, N, 128, seed=M)
+        x, w, z, s = (torch.from_numpy(p[k]).to(DEV) for k in ("x", "qweight", "qzeros", "scales"))
+        return lambda: awq.gemm(x, w, z, s, None, 128)
+
+    calls = [attention(3000, 3, 8, 2), attention(5000, 40, 32, 8), product(16, 14336, 4096),
+             product(1, 8192, 7168)]
+    want = [f() for f in calls]
+    torch.cuda.synchronize()
+    wrong, failed = [], []
+
+    def work(x):
+        try:
+            for _ in range(30):
+                if not torch.equal(calls[x](), want[x]):
+                    wrong.append(x)
+        except Exception as e:   # reported by the thread that waits
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(x,)) for x in range(len(calls))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    torch.cuda.synchronize()
+    assert not failed and not wrong and not any(t.is_alive() for t in threads), (failed, wrong)

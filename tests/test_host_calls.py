@@ -1,0 +1,91 @@
+"""What a call does on the host around its launches, without a GPU: the
+library and its binding run against a stand-in for HIP's launch and device
+calls (tests/native/hip_stub.cpp), in a process of their own."""
+import os
+import subprocess
+import sys
+import textwrap
+
+import pytest
+
+from bit_weight_quantized_awq_amd import build
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def stub(tmp_path_factory):
+    """The stand-in, built."""
+    path = str(tmp_path_factory.mktemp("stub") / "hip_stub.so")
+    include = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(build.hipcc()))), "include")
+    cmd = ["g++", "-std=c++17", "-O1", "-shared", "-fPIC", "-D__HIP_PLATFORM_AMD__=1", "-isystem",
+           include, os.path.join(ROOT, "tests", "native", "hip_stub.cpp"), "-o", path]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    assert res.returncode == 0, res.stderr
+    return path
+
+
+PRELUDE = """
+import ctypes, sys, threading
+stub = ctypes.CDLL(sys.argv[1], mode=ctypes.RTLD_GLOBAL)
+stub.stub_thread.restype = ctypes.c_uint64
+"""
+
+
+def run(stub, program):
+    """Runs `program` after the stand-in has been loaded; it prints "ok"."""
+    res = subprocess.run([sys.executable, "-c", PRELUDE + textwrap.dedent(program), stub], cwd=ROOT,
+                         capture_output=True, text=True, timeout=300)
+    assert res.returncode == 0 and res.stdout.endswith("ok\n"), res.stdout + res.stderr
+
+
+def test_calls_that_share_a_workspace_are_not_interleaved(stub):
+    """Kernels of a call that hand each other data through the workspace are
+    launched one after the other, whatever other host threads launch."""
+    run(stub, """
+        import bit_weight_quantized_awq_amd as awq
+        from bit_weight_quantized_awq_amd import binding as b
+        A, WS = 0x10000, 0x100000
+        c = b.KvCacheStruct(k=A, v=A, num_blocks=1000, block_size=16, heads=8, head_dim=128,
+                            k_block_stride=16384, k_slot_stride=1024, k_head_stride=128,
+                            v_block_stride=16384, v_slot_stride=1024, v_head_stride=128)
+        lib = awq.lib()
+
+        def attention():     # the kernel and the join
+            return lib.awq_tree_attention(A, ctypes.byref(c), A, A, A, None, A, 2, 4, 32, 100, 100,
+                                          0, 4096, 128, 0.1, b.AWQ_F16, WS, 1 << 40, None)
+
+        def product():       # split along K, and the sum
+            return lib.awq_gemm(A, A, A, A, None, A, 16, 14336, 4096, 128, WS, 1 << 40, None)
+
+        def gathered():      # the reordered x, the product and its sum
+            return lib.awq_gemm_sorted(A, A, A, A, A, None, A, 128, 4096, 4096, 4096, 128, WS,
+                                       1 << 40, None)
+
+        for f, n in ((attention, 2), (product, 2), (gathered, 3)):
+            stub.stub_clear()
+            assert f() == 0 and stub.stub_launches() == n, (f.__name__, stub.stub_launches())
+
+        stub.stub_clear()
+        calls = {attention: 2, product: 2, gathered: 3}
+        names, failed = {}, []
+
+        def work(f):
+            names[threading.get_ident()] = calls[f]
+            for _ in range(40):
+                if f() != 0:
+                    failed.append(f)
+
+        threads = [threading.Thread(target=work, args=(f,)) for f in calls for _ in range(2)]
+        for t in threads: t.start()
+        for t in threads: t.join()
+        assert not failed
+        order = [stub.stub_thread(i) for i in range(stub.stub_launches())]
+        assert len(order) == 2 * 40 * 7
+        i = 0
+        while i < len(order):
+            n = names[order[i]]
+            assert order[i:i + n] == [order[i]] * n, (i, order[i:i + n])
+            i += n
+        print("ok")
+        """)
