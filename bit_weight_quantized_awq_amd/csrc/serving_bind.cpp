@@ -10,6 +10,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/hip/HIPGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/DynamicTypes.h>
@@ -120,9 +121,12 @@ PyObject* guarded(Py_ssize_t given, Py_ssize_t wanted, F f) {
   }
   return nullptr;
 }
-// The C call without the interpreter's lock, as ctypes makes it.
+// The C call without the interpreter's lock, as ctypes makes it, and with the
+// tensors' device current: a launch goes to the current one, and the null
+// stream is that one's.
 template <class F>
-int unlocked(F f) {
+int unlocked(at::Device device, F f) {
+  const c10::hip::HIPGuard guard(device.index());
   PyThreadState* state = PyEval_SaveThread();
   const int st = f();
   PyEval_RestoreThread(state);
@@ -169,7 +173,7 @@ PyObject* batch_layout(PyObject*, PyObject* const* args, Py_ssize_t count) {
     }
     int32_t* p = whole.data_ptr<int32_t>();
     void* stream = stream_of(device);
-    const int st = unlocked([&] {
+    const int st = unlocked(device, [&] {
       return awq_batch_layout(cached.data_ptr(), counts.data_ptr(), held.data_ptr(),
                               free.data_ptr(), pointer(start), pointer(parents), table.data_ptr(),
                               p + 3 * T, p, p + T, p + 2 * T, words ? mask.data_ptr() : nullptr,
@@ -250,7 +254,7 @@ PyObject* kv_write(PyObject*, PyObject* const* args, Py_ssize_t count) {
     const at::IntArrayRef ks = k.strides(), vs = v.strides();
     if (ks[2] != 1 || vs[2] != 1) value_error("the channels of k and v must be contiguous");
     void* stream = stream_of(device);
-    return status(unlocked([&] {
+    return status(unlocked(device, [&] {
       return awq_kv_write(T ? k.data_ptr() : nullptr, T ? v.data_ptr() : nullptr,
                           T ? slots.data_ptr() : nullptr, &cache, T, ks[0], ks[1], vs[0], vs[1],
                           dtype, stream);
@@ -336,7 +340,7 @@ PyObject* tree_attention(PyObject*, PyObject* const* args, Py_ssize_t count) {
     void* const ws_data = ws ? ws->data_ptr() : nullptr;
     const size_t ws_bytes = ws ? ws->nbytes() : 0;
     const Tensor out = given ? *given : new_tensor({T, heads, dim}, q.scalar_type(), device);
-    const int st = unlocked([&] {
+    const int st = unlocked(device, [&] {
       return awq_tree_attention(T ? q.data_ptr() : nullptr, &cache, table.data_ptr(),
                                 cached.data_ptr(), q_start.data_ptr(), pointer(mask),
                                 T ? out.data_ptr() : nullptr, B, T, heads, W, table.stride(0), words,
@@ -460,7 +464,7 @@ PyObject* process_logits(PyObject*, PyObject* const* args, Py_ssize_t count) {
     a.out = R ? out.data_ptr() : nullptr;
     a.out_stride = out.stride(0);
     void* stream = stream_of(device);
-    const int st = unlocked([&] { return awq_process_logits(&a, stream); });
+    const int st = unlocked(device, [&] { return awq_process_logits(&a, stream); });
     if (st != AWQ_SUCCESS) return status(st);
     if (given) {
       Py_INCREF(args[14]);

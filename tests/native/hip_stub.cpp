@@ -5,6 +5,8 @@
 #include <hip/hip_runtime_api.h>
 
 #include <pthread.h>
+#include <stddef.h>
+#include <stdlib.h>
 #include <unistd.h>
 
 #include <mutex>
@@ -64,6 +66,15 @@ hipError_t hipSetDevice(int d) {
   current = d;
   return hipSuccess;
 }
+hipError_t hipDeviceGetStreamPriorityRange(int* least, int* greatest) {
+  *least = *greatest = 0;
+  return hipSuccess;
+}
+// The allocator of torch's tensors, from host memory.
+void* stub_alloc(ptrdiff_t bytes, int, hipStream_t) {
+  return aligned_alloc(512, (bytes + 511) / 512 * 512);
+}
+void stub_free(void* p, ptrdiff_t, int, hipStream_t) { free(p); }
 
 int stub_launches(void) {
   std::lock_guard<std::mutex> hold(lock);

@@ -89,3 +89,39 @@ def test_calls_that_share_a_workspace_are_not_interleaved(stub):
             i += n
         print("ok")
         """)
+
+
+DEVICES = """
+import torch
+# Tensors of two devices that are not there, in host memory.
+torch.cuda._initialized = True
+torch.cuda.memory.change_current_allocator(
+    torch.cuda.memory.CUDAPluggableAllocator(sys.argv[1], "stub_alloc", "stub_free"))
+import bit_weight_quantized_awq_amd as awq
+F16, I32, I64 = torch.float16, torch.int32, torch.int64
+
+def new(*shape, dtype=I32, device="cuda:1"):
+    return torch.empty(shape, dtype=dtype, device=device)
+
+def on_one(call, launches=1):
+    # A call on tensors of device 1, with device 0 current.
+    assert torch.cuda.current_device() == 0
+    stub.stub_clear()
+    call()
+    seen = [stub.stub_device(i) for i in range(stub.stub_launches())]
+    assert seen == [1] * launches, seen
+    assert torch.cuda.current_device() == 0
+"""
+
+
+def test_serving_calls_launch_on_their_tensors_device(stub):
+    run(stub, DEVICES + textwrap.dedent("""
+        k, q, cache = new(4, 2, 64, dtype=F16), new(4, 8, 64, dtype=F16), new(10, 16, 2, 64, dtype=F16)
+        two, three = new(2), new(3)
+        on_one(lambda: awq.batch_layout(two, two, two, new(5), new(2, 4), 16, 10, 4))
+        on_one(lambda: awq.kv_write(k, k, new(4), cache, cache))
+        ws = new(1 << 24, dtype=torch.uint8)
+        on_one(lambda: awq.tree_attention(q, cache, cache, new(2, 400), two, three, workspace=ws), 2)
+        on_one(lambda: awq.process_logits(new(4, 500, dtype=F16)))
+        print("ok")
+        """))
