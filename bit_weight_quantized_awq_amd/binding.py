@@ -301,10 +301,30 @@ def _workspace(device, stream_ptr: int, nbytes: int):
         return buf
 
 
+_get_stream = _get_device = None   # torch's functions, once torch has been imported
+
+
 def _current_stream(device):
     """The raw hipStream_t of the current stream on `device`."""
-    torch = _torch()
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    global _get_stream, _get_device
+    if _get_stream is None:
+        torch = _torch()
+        _get_device = torch._C._cuda_getDevice
+        _get_stream = torch._C._cuda_getCurrentRawStream
+    return _get_stream(device.index)
+
+
+def _run(fn, where, device, *args):
+    """Calls the entry point fn with `device` current and raises for a status:
+    a launch goes to the current device, and the null stream is that one's.
+    The stream among the arguments is from _current_stream."""
+    if _get_device() == device.index:
+        st = fn(*args)
+    else:
+        with _torch().cuda.device(device):
+            st = fn(*args)
+    if st != AWQ_SUCCESS:
+        raise AwqError(st, where)
 
 
 def _check_device(name, t, device):
@@ -371,12 +391,9 @@ def gemm(x, qweight, qzeros, scales, bias=None, group_size: int = 128, out=None,
         ws = workspace
     ws_ptr = ws.data_ptr() if ws is not None else None
     ws_bytes = ws.numel() * ws.element_size() if ws is not None else 0
-    st = lib().awq_gemm(x2.data_ptr() if M else None, qweight.data_ptr(), qzeros.data_ptr(),
-                        scales.data_ptr(), bias.data_ptr() if bias is not None else None,
-                        y.data_ptr() if M else None, M, K, N, group_size, ws_ptr, ws_bytes,
-                        stream)
-    if st != AWQ_SUCCESS:
-        raise AwqError(st, "awq_gemm")
+    _run(lib().awq_gemm, "awq_gemm", device, x2.data_ptr() if M else None, qweight.data_ptr(),
+         qzeros.data_ptr(), scales.data_ptr(), bias.data_ptr() if bias is not None else None,
+         y.data_ptr() if M else None, M, K, N, group_size, ws_ptr, ws_bytes, stream)
     return y.reshape(*lead, N)
 
 
@@ -404,13 +421,10 @@ def gemm_noalloc(x, qweight, qzeros, scales, bias=None, group_size: int = 128, o
     lead, x2 = _prep_x(x, K)
     M = x2.shape[0]
     y = _prep_out(out, M, N, device)
-    st = lib().awq_gemm_noalloc(x2.data_ptr() if M else None, qweight.data_ptr(),
-                                qzeros.data_ptr(), scales.data_ptr(),
-                                bias.data_ptr() if bias is not None else None,
-                                y.data_ptr() if M else None, M, K, N, group_size,
-                                _current_stream(device))
-    if st != AWQ_SUCCESS:
-        raise AwqError(st, "awq_gemm_noalloc")
+    _run(lib().awq_gemm_noalloc, "awq_gemm_noalloc", device, x2.data_ptr() if M else None,
+         qweight.data_ptr(), qzeros.data_ptr(), scales.data_ptr(),
+         bias.data_ptr() if bias is not None else None, y.data_ptr() if M else None, M, K, N,
+         group_size, _current_stream(device))
     return y.reshape(*lead, N)
 
 
@@ -443,11 +457,9 @@ def dense_gemv(x, w, bias=None, out=None):
         if out.shape != (M, N) or out.dtype != torch.float16 or not out.is_contiguous():
             raise ValueError("out must be a contiguous float16 (M, N) tensor")
     stream = _current_stream(device)
-    st = lib().awq_dense_gemv(x2.data_ptr() if M else None, w.data_ptr(),
-                              bias.data_ptr() if bias is not None else None,
-                              y.data_ptr() if M else None, M, K, N, stream)
-    if st != AWQ_SUCCESS:
-        raise AwqError(st, "awq_dense_gemv")
+    _run(lib().awq_dense_gemv, "awq_dense_gemv", device, x2.data_ptr() if M else None,
+         w.data_ptr(), bias.data_ptr() if bias is not None else None,
+         y.data_ptr() if M else None, M, K, N, stream)
     return y.reshape(*lead, N)
 
 
@@ -471,10 +483,8 @@ def dequant(qweight, qzeros, scales, group_size: int = 128, out=None):
             raise ValueError("out must be a contiguous float16 (K, N) tensor")
     w = out if out is not None else torch.empty((K, N), dtype=torch.float16, device=device)
     stream = _current_stream(device)
-    st = lib().awq_dequant(qweight.data_ptr(), qzeros.data_ptr(), scales.data_ptr(),
-                           w.data_ptr(), K, N, group_size, stream)
-    if st != AWQ_SUCCESS:
-        raise AwqError(st, "awq_dequant")
+    _run(lib().awq_dequant, "awq_dequant", device, qweight.data_ptr(), qzeros.data_ptr(),
+         scales.data_ptr(), w.data_ptr(), K, N, group_size, stream)
     return w
 
 
@@ -517,10 +527,8 @@ def dequant_gidx(qweight, qzeros, scales, g_idx, out=None):
             raise ValueError("out must be a contiguous float16 (K, N) tensor")
     w = out if out is not None else torch.empty((K, N), dtype=torch.float16, device=device)
     stream = _current_stream(device)
-    st = lib().awq_dequant_gidx(qweight.data_ptr(), qzeros.data_ptr(), scales.data_ptr(),
-                                g_idx.data_ptr(), w.data_ptr(), K, N, G, stream)
-    if st != AWQ_SUCCESS:
-        raise AwqError(st, "awq_dequant_gidx")
+    _run(lib().awq_dequant_gidx, "awq_dequant_gidx", device, qweight.data_ptr(),
+         qzeros.data_ptr(), scales.data_ptr(), g_idx.data_ptr(), w.data_ptr(), K, N, G, stream)
     return w
 
 
@@ -565,12 +573,10 @@ def gemm_gidx(x, qweight, qzeros, scales, g_idx, bias=None, out=None):
     y = _prep_out(out, M, N, device)
     qweight, qzeros, scales = qweight.contiguous(), qzeros.contiguous(), scales.contiguous()
     stream = _current_stream(device)
-    st = lib().awq_gemm_gidx(x2.data_ptr() if M else None, qweight.data_ptr(),
-                             qzeros.data_ptr(), scales.data_ptr(), g_idx.data_ptr(),
-                             bias.data_ptr() if bias is not None else None,
-                             y.data_ptr() if M else None, M, K, N, G, stream)
-    if st != AWQ_SUCCESS:
-        raise AwqError(st, "awq_gemm_gidx")
+    _run(lib().awq_gemm_gidx, "awq_gemm_gidx", device, x2.data_ptr() if M else None,
+         qweight.data_ptr(), qzeros.data_ptr(), scales.data_ptr(), g_idx.data_ptr(),
+         bias.data_ptr() if bias is not None else None, y.data_ptr() if M else None, M, K, N, G,
+         stream)
     return y.reshape(*lead, N)
 
 
@@ -607,10 +613,8 @@ def gather_rows(src, idx, out=None):
         if out.shape != (rows, src.shape[1]) or out.dtype != src.dtype or not out.is_contiguous():
             raise ValueError("out must be a contiguous tensor of shape (len(idx), src.shape[1])")
     stream = _current_stream(device)
-    st = lib().awq_gather_rows(src.data_ptr(), src.shape[0], idx.data_ptr(), out.data_ptr(),
-                               rows, row_bytes, stream)
-    if st != AWQ_SUCCESS:
-        raise AwqError(st, "awq_gather_rows")
+    _run(lib().awq_gather_rows, "awq_gather_rows", device, src.data_ptr(), src.shape[0],
+         idx.data_ptr(), out.data_ptr(), rows, row_bytes, stream)
     return out
 
 
@@ -683,11 +687,8 @@ def gemm_sorted(x, w, bias=None, out=None, workspace=None):
     ws = _workspace(device, stream, need) if workspace is None else workspace
     ws_ptr = ws.data_ptr() if ws is not None else None
     ws_bytes = ws.numel() * ws.element_size() if ws is not None else 0
-    st = lib().awq_gemm_sorted(x2.data_ptr() if M else None, w.perm.data_ptr(),
-                               w.qweight.data_ptr(), w.qzeros.data_ptr(), w.scales.data_ptr(),
-                               bias.data_ptr() if bias is not None else None,
-                               y.data_ptr() if M else None, M, K_in, rows, N, w.block_rows,
-                               ws_ptr, ws_bytes, stream)
-    if st != AWQ_SUCCESS:
-        raise AwqError(st, "awq_gemm_sorted")
+    _run(lib().awq_gemm_sorted, "awq_gemm_sorted", device, x2.data_ptr() if M else None,
+         w.perm.data_ptr(), w.qweight.data_ptr(), w.qzeros.data_ptr(), w.scales.data_ptr(),
+         bias.data_ptr() if bias is not None else None, y.data_ptr() if M else None, M, K_in,
+         rows, N, w.block_rows, ws_ptr, ws_bytes, stream)
     return y.reshape(*lead, N)

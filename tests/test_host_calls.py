@@ -125,3 +125,25 @@ def test_serving_calls_launch_on_their_tensors_device(stub):
         on_one(lambda: awq.process_logits(new(4, 500, dtype=F16)))
         print("ok")
         """))
+
+
+def test_linear_calls_launch_on_their_tensors_device(stub):
+    run(stub, DEVICES + textwrap.dedent("""
+        K, N, g = 256, 128, 64
+        x, w = new(2, K, dtype=F16), new(K, N // 8)
+        z, s, y = new(K // g, N // 8), new(K // g, N, dtype=F16), new(2, N, dtype=F16)
+        ws, gidx = new(1 << 24, dtype=torch.uint8), new(K)
+        on_one(lambda: awq.gemm(x, w, z, s, None, g, workspace=ws))
+        # The first one clears the scratch of its device.
+        on_one(lambda: awq.gemm_noalloc(x, w, z, s, None, g), 2)
+        on_one(lambda: awq.gemm_noalloc(x, w, z, s, None, g))
+        on_one(lambda: awq.dequant(w, z, s, g))
+        on_one(lambda: awq.dequant_gidx(w, z, s, gidx))
+        on_one(lambda: awq.gemm_gidx(x, w, z, s, gidx))
+        on_one(lambda: awq.gather_rows(w, new(5)))
+        on_one(lambda: awq.dense_gemv(x, new(N, K, dtype=F16)))
+        # The x that a batch of 64 rows reorders, and the product.
+        sorted_w = awq.SortedWeight(w, z, s, gidx, g, K)
+        on_one(lambda: awq.gemm_sorted(new(64, K, dtype=F16), sorted_w, workspace=ws), 2)
+        print("ok")
+        """))
