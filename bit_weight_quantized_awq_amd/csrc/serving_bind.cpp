@@ -123,14 +123,16 @@ PyObject* guarded(Py_ssize_t given, Py_ssize_t wanted, F f) {
 }
 // The C call without the interpreter's lock, as ctypes makes it, and with the
 // tensors' device current: a launch goes to the current one, and the null
-// stream is that one's.
+// stream is that one's.  f reads no tensor: another thread may change one, and
+// one without memory throws.
 template <class F>
 int unlocked(at::Device device, F f) {
   const c10::hip::HIPGuard guard(device.index());
-  PyThreadState* state = PyEval_SaveThread();
-  const int st = f();
-  PyEval_RestoreThread(state);
-  return st;
+  const struct Release {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Release() { PyEval_RestoreThread(state); }
+  } release;
+  return f();
 }
 PyObject* status(int st) { return PyLong_FromLong(st); }
 
@@ -172,12 +174,14 @@ PyObject* batch_layout(PyObject*, PyObject* const* args, Py_ssize_t count) {
       at += sizes[i];
     }
     int32_t* p = whole.data_ptr<int32_t>();
+    const void *pc = cached.data_ptr(), *pn = counts.data_ptr(), *ph = held.data_ptr(),
+               *pf = free.data_ptr(), *ps = pointer(start), *pp = pointer(parents);
+    void *pt = table.data_ptr(), *pm = words ? mask.data_ptr() : nullptr;
+    const int64_t num_free = free.numel();
     void* stream = stream_of(device);
     const int st = unlocked(device, [&] {
-      return awq_batch_layout(cached.data_ptr(), counts.data_ptr(), held.data_ptr(),
-                              free.data_ptr(), pointer(start), pointer(parents), table.data_ptr(),
-                              p + 3 * T, p, p + T, p + 2 * T, words ? mask.data_ptr() : nullptr,
-                              p + 3 * T + B + 1, p + 3 * T + 2 * B + 1, B, T, free.numel(), W,
+      return awq_batch_layout(pc, pn, ph, pf, ps, pp, pt, p + 3 * T, p, p + T, p + 2 * T, pm,
+                              p + 3 * T + B + 1, p + 3 * T + 2 * B + 1, B, T, num_free, W,
                               block_size, num_blocks, words, stream);
     });
     if (st != AWQ_SUCCESS) return status(st);
@@ -253,11 +257,11 @@ PyObject* kv_write(PyObject*, PyObject* const* args, Py_ssize_t count) {
     need("slots", slots, at::kInt, {T}, device);
     const at::IntArrayRef ks = k.strides(), vs = v.strides();
     if (ks[2] != 1 || vs[2] != 1) value_error("the channels of k and v must be contiguous");
+    const void *pk = k.data_ptr(), *pv = v.data_ptr(), *ps = slots.data_ptr();
+    const int64_t kts = ks[0], khs = ks[1], vts = vs[0], vhs = vs[1];
     void* stream = stream_of(device);
     return status(unlocked(device, [&] {
-      return awq_kv_write(T ? k.data_ptr() : nullptr, T ? v.data_ptr() : nullptr,
-                          T ? slots.data_ptr() : nullptr, &cache, T, ks[0], ks[1], vs[0], vs[1],
-                          dtype, stream);
+      return awq_kv_write(pk, pv, ps, &cache, T, kts, khs, vts, vhs, dtype, stream);
     }));
   });
 }
@@ -340,11 +344,13 @@ PyObject* tree_attention(PyObject*, PyObject* const* args, Py_ssize_t count) {
     void* const ws_data = ws ? ws->data_ptr() : nullptr;
     const size_t ws_bytes = ws ? ws->nbytes() : 0;
     const Tensor out = given ? *given : new_tensor({T, heads, dim}, q.scalar_type(), device);
+    const void *pq = q.data_ptr(), *pt = table.data_ptr(), *pc = cached.data_ptr(),
+               *ps = q_start.data_ptr(), *pm = pointer(mask);
+    void* po = out.data_ptr();
+    const int64_t row = table.stride(0), qts = qs[0], qhs = qs[1];
     const int st = unlocked(device, [&] {
-      return awq_tree_attention(T ? q.data_ptr() : nullptr, &cache, table.data_ptr(),
-                                cached.data_ptr(), q_start.data_ptr(), pointer(mask),
-                                T ? out.data_ptr() : nullptr, B, T, heads, W, table.stride(0), words,
-                                qs[0], qs[1], scale, dtype, ws_data, ws_bytes, stream);
+      return awq_tree_attention(pq, &cache, pt, pc, ps, pm, po, B, T, heads, W, row, words, qts, qhs,
+                                scale, dtype, ws_data, ws_bytes, stream);
     });
     if (st != AWQ_SUCCESS) return status(st);
     if (given) {

@@ -147,3 +147,43 @@ def test_linear_calls_launch_on_their_tensors_device(stub):
         on_one(lambda: awq.gemm_sorted(new(64, K, dtype=F16), sorted_w, workspace=ws), 2)
         print("ok")
         """))
+
+
+def test_tensors_without_memory_raise(stub):
+    """Operands that hold no memory (fake ones, as tracers make them) end in
+    an exception, not in a process without the interpreter's lock."""
+    run(stub, DEVICES + textwrap.dedent("""
+        def none(*shape, dtype=I32):
+            t = new(*shape, dtype=dtype)
+            torch._C._set_throw_on_mutable_data_ptr(t)
+            return t
+
+        k, q, cache = new(4, 2, 64, dtype=F16), new(4, 8, 64, dtype=F16), new(10, 16, 2, 64, dtype=F16)
+        two, three, table = new(2), new(3), new(2, 4)
+        ws = new(1 << 24, dtype=torch.uint8)
+        for call in [
+                lambda: awq.batch_layout(none(2), two, two, new(5), table, 16, 10, 4),
+                lambda: awq.batch_layout(two, two, two, new(5), none(2, 4), 16, 10, 4),
+                lambda: awq.kv_write(none(4, 2, 64, dtype=F16), k, new(4), cache, cache),
+                lambda: awq.kv_write(k, k, none(4), cache, cache),
+                lambda: awq.kv_write(k, k, new(4), none(10, 16, 2, 64, dtype=F16), cache),
+                lambda: awq.tree_attention(none(4, 8, 64, dtype=F16), cache, cache, table, two, three,
+                                           workspace=ws),
+                lambda: awq.tree_attention(q, cache, cache, none(2, 4), two, three, workspace=ws),
+                lambda: awq.tree_attention(q, cache, cache, table, two, none(3), workspace=ws),
+                lambda: awq.tree_attention(q, cache, cache, table, two, three,
+                                           workspace=none(1 << 24, dtype=torch.uint8)),
+                lambda: awq.process_logits(none(4, 500, dtype=F16)),
+                lambda: awq.process_logits(new(4, 500, dtype=F16), requests=none(4))]:
+            stub.stub_clear()
+            try:
+                call()
+            except RuntimeError as e:
+                pass
+            else:
+                raise AssertionError("no exception")
+            assert stub.stub_launches() == 0
+            assert torch.cuda.current_device() == 0
+        on_one(lambda: awq.kv_write(k, k, new(4), cache, cache))
+        print("ok")
+        """))
