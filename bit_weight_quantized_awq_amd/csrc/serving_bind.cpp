@@ -76,6 +76,13 @@ void need(const char* name, const Tensor& t, at::ScalarType dtype, at::IntArrayR
     value_error(std::string(name) + " must have shape " + text(shape) + ", got " + text(t.sizes()));
   if (!t.is_contiguous()) value_error(std::string(name) + " must be contiguous");
 }
+// Words of the masks of n tokens, at least one: no words would be no mask.
+int64_t need_mask(const Tensor& t, int64_t n, at::Device device) {
+  const int64_t words = t.dim() ? t.size(-1) : 0;
+  need("tree_mask", t, at::kLong, {n, words}, device);
+  if (words == 0 && n > 0) value_error("tree_mask must have a word or more for each token");
+  return words;
+}
 const void* pointer(const Tensor* t) { return t ? t->data_ptr() : nullptr; }
 
 int act_dtype(at::ScalarType t) {
@@ -317,12 +324,8 @@ PyObject* tree_attention(PyObject*, PyObject* const* args, Py_ssize_t count) {
     if (table.stride(1) != 1 && W > 1) value_error("the rows of block_table must be contiguous");
     need("cached_lens", cached, at::kInt, {B}, device);
     need("q_start", q_start, at::kInt, {B + 1}, device);
-    int64_t words = 0;
     const Tensor* mask = maybe("tree_mask", args[6]);
-    if (mask) {
-      words = mask->dim() ? mask->size(-1) : 0;
-      need("tree_mask", *mask, at::kLong, {T, words}, device);
-    }
+    const int64_t words = mask ? need_mask(*mask, T, device) : 0;
     double scale = 0.0;
     if (args[9] == Py_None) {
       scale = 1.0 / std::sqrt(static_cast<double>(dim));
@@ -455,9 +458,8 @@ PyObject* process_logits(PyObject*, PyObject* const* args, Py_ssize_t count) {
     if (draft || mask || q_start) {
       if (!draft || !mask || !q_start)
         value_error("draft_tokens, tree_mask and q_start come together");
-      const int64_t words = mask->dim() ? mask->size(-1) : 0;
       need("draft_tokens", *draft, at::kInt, {R}, device);
-      need("tree_mask", *mask, at::kLong, {R, words}, device);
+      const int64_t words = need_mask(*mask, R, device);
       need("q_start", *q_start, at::kInt, {B + 1}, device);
       if (R) {
         a.draft_tokens = draft->data_ptr();

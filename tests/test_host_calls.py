@@ -187,3 +187,28 @@ def test_tensors_without_memory_raise(stub):
         on_one(lambda: awq.kv_write(k, k, new(4), cache, cache))
         print("ok")
         """))
+
+
+def test_masks_of_no_words_are_refused(stub):
+    """A mask that has no bits is no causal chain."""
+    run(stub, DEVICES + textwrap.dedent("""
+        q, cache = new(4, 8, 64, dtype=F16), new(10, 16, 2, 64, dtype=F16)
+        ws = new(1 << 24, dtype=torch.uint8)
+        stub.stub_clear()
+        try:
+            awq.tree_attention(q, cache, cache, new(2, 4), new(2), new(3), tree_mask=new(4, 0, dtype=I64),
+                               workspace=ws)
+        except ValueError as e:
+            assert "tree_mask" in str(e)
+        else:
+            raise AssertionError("no exception")
+        try:
+            awq.process_logits(new(4, 50, dtype=F16), requests=new(4), draft_tokens=new(4),
+                               tree_mask=new(4, 0, dtype=I64), q_start=new(3))
+        except ValueError as e:
+            assert "tree_mask" in str(e)
+        else:
+            raise AssertionError("no exception")
+        assert stub.stub_launches() == 0
+        print("ok")
+        """))
