@@ -106,10 +106,12 @@ __device__ __forceinline__ v4i raw_rsrc(const void* base, uint32_t bytes) {
 // awaited with explicit vmcnt waits that tie the loaded registers, so nothing
 // reads them earlier.
 //
-// 16-byte HBM -> LDS copy per lane (lane i writes lds + 16 * i).
+// 16-byte HBM -> LDS copy per lane (lane i writes lds + 16 * i).  A copy must
+// not follow a scalar write of m0 directly (one wait state), which the compiler
+// sees to for its own instructions only.
 __device__ __forceinline__ void copy_to_lds(v4i rsrc, uint32_t voff, uint32_t soff,
                                             uint32_t lds) {
-  asm volatile("buffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(voff), "s"(rsrc), "s"(soff),
+  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(voff), "s"(rsrc), "s"(soff),
                "{m0}"(lds)
                : "memory");
 }
