@@ -141,3 +141,60 @@ def test_host_threads_on_one_stream():
         t.join(60)
     torch.cuda.synchronize()
     assert not failed and not wrong and not any(t.is_alive() for t in threads), (failed, wrong)
+
+
+# ----------------------------------------------------------------------------- tree_attention
+from test_gpu_serving import E4M3, HALF, TINY, Problem, wide  # noqa: E402
+
+F16, BF16 = torch.float16, torch.bfloat16
+# (heads, key heads, contexts, tokens): 16, 32 and 128 rows of a key head, runs
+# of many tiles that several work-groups join.
+ROWS = [(4, 2, [700, 3, 90], [2, 1, 3]), (8, 2, [2500, 40], [6, 4]), (32, 2, [1500, 0], [9, 5])]
+
+
+def fill(p, k, v):
+    """Keys and values (rows in the order of the requests, heads, D) into the cache."""
+    slots = [p.table[b, j // p.bs] * p.bs + j % p.bs for b in range(len(p.ctx))
+             for j in range(p.ctx[b] + p.added[b])]
+    one = None if p.k_scale is None else torch.ones(p.kvh, device=DEV)
+    awq.kv_write(k.to(p.dtype), v.to(p.dtype), i32(slots), p.kc, p.vc, one, one)
+    if one is not None:
+        p.k_scale, p.v_scale = one, one
+
+
+@pytest.mark.parametrize("heads,kvh,ctx,added", ROWS)
+@pytest.mark.parametrize("dtype,e4m3", [(F16, False), (BF16, False), (F16, True), (BF16, True)])
+@pytest.mark.parametrize("scale", [2.0 ** 16, -2.0 ** 22, 2.0 ** 26, 2.0 ** 100])
+def test_attention_huge_scores(heads, kvh, ctx, added, dtype, e4m3, scale):
+    """Scores that are exact and so far apart that the largest ones alone have
+    weights: the mean of their values, however large the scores are.
+
+    Whole numbers below 16 in the queries and keys: every product and sum is
+    exact in float32, and scores that differ do so by 2^16 at least, where
+    float32's step at the largest (2^16 times 16 * 16 * 64) is 2^7 of the
+    same.  Equal scores have equal weights.  What is left is the rounding of
+    the sum of up to `ties` values, of the quotient and of the output."""
+    p = Problem(ctx, added, heads, kvh, 64, 16, dtype, e4m3, tree=True, seed=heads)
+    say(f"huge scores heads={heads}/{kvh} {dtype} e4m3={e4m3} scale={scale}")
+    rng = np.random.default_rng(heads)
+    rows = sum(ctx) + sum(added)
+    k, v = (torch.from_numpy(rng.integers(-15, 16, (rows, kvh, 64))).to(torch.float32).to(DEV)
+            for _ in range(2))
+    fill(p, k, v)
+    p.q[:] = torch.from_numpy(rng.integers(-15, 16, p.q.shape)).to(dtype).to(DEV)
+    got = wide(p.run(scale=scale))
+    kc, vc, q = wide(p.kc), wide(p.vc), wide(p.q)
+    bs, G = p.bs, heads // kvh
+    for b in range(len(ctx)):
+        j = np.arange(ctx[b] + added[b])
+        page, off = p.table[b, j // bs], j % bs
+        for t in range(p.q_start[b], p.q_start[b + 1]):
+            bits = int(p.mask[t, 0])
+            see = (j < ctx[b]) | np.array([bool(bits >> int(max(x - ctx[b], 0)) & 1) for x in j])
+            for h in range(heads):
+                s = (kc[page, off, h // G] @ q[t, h]) * np.sign(scale)
+                best = see & (s == s[see].max())
+                x = vc[page, off, h // G][best]
+                want, size = x.mean(0), np.abs(x).mean(0)
+                lim = len(x) * 2.0 ** -22 * size + HALF[dtype] * 1.01 * np.abs(want) + TINY[dtype]
+                assert (np.abs(got[t, h] - want) <= lim).all(), (b, t, h, got[t, h][:4], want[:4])
