@@ -86,7 +86,7 @@ struct AttentionLaunch {
   // (2 * groups slots of R rows), and which row block it is the first of.
   float* sums;          // [slot][row][channel]
   RowStat* stats;       // [slot][row]: reference, sum of weights
-  int32_t* owners;      // [group][kOwnerWords]: parts, start, head, first row, rows; then
+  int32_t* owners;      // [group][kOwnerWords]: parts, start, head, first row, rows, request; then
                         // the number of work-groups that had units; unused
                         // by one team, whose row blocks are whole
 };

@@ -198,3 +198,36 @@ def test_attention_huge_scores(heads, kvh, ctx, added, dtype, e4m3, scale):
                 want, size = x.mean(0), np.abs(x).mean(0)
                 lim = len(x) * 2.0 ** -22 * size + HALF[dtype] * 1.01 * np.abs(want) + TINY[dtype]
                 assert (np.abs(got[t, h] - want) <= lim).all(), (b, t, h, got[t, h][:4], want[:4])
+
+
+@pytest.mark.parametrize("heads,kvh,ctx,added", ROWS)
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_attention_scores_of_minus_infinity(heads, kvh, ctx, added, dtype):
+    """Keys that overflowed to a score of -infinity: a row that sees nothing
+    else is NaN, as the softmax of its scores; beside finite scores they have
+    no weight; a row that sees nothing at all stays 0."""
+    p = Problem(ctx, added, heads, kvh, 64, 16, dtype, tree=True, seed=heads + 1)
+    say(f"scores of -infinity heads={heads}/{kvh} {dtype}")
+    p.q[:, :, 0] = 1.0
+    last = len(ctx) - 1
+    for b in range(len(ctx)):
+        for j in range(ctx[b] + added[b]):
+            if b == 0 and j % 7 == 0:
+                continue
+            p.kc[int(p.table[b, j // 16]), j % 16, :, 0] = float("-inf")
+    if ctx[last] == 0:
+        p.mask[p.q_start[last]] = 0
+    got = wide(p.run())
+    out, weight, spread, keys = p.want()
+    assert (keys > 0)[:p.q_start[last]].all()
+    other = np.arange(p.T) >= p.q_start[1]
+    nothing = keys == 0
+    assert (got[nothing] == 0).all()
+    assert np.isnan(out[other & ~nothing]).all()
+    assert np.isnan(got[other & ~nothing]).all()
+    first = slice(0, p.q_start[1])
+    assert np.isfinite(got[first]).all()
+    # As Problem.bound, with the spread of the finite scores.
+    spread = np.full_like(spread, 64 * 12.0 * 6.0 * p.scale)
+    lim = p.bound(out, weight, spread, keys)
+    assert (np.abs(got - out)[first] <= lim[first]).all()
