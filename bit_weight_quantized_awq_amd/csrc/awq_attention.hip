@@ -326,33 +326,38 @@ __device__ __forceinline__ void tile_step(const AttentionArgs& a, const Place& a
   }
   scored();
 
+  // The keys of the tile that the lane's row sees.
+  auto seen_by = [&](int nt) -> uint32_t {
+    uint32_t bits = here;
+    if constexpr (DRAFTED) {
+      const int r = 16 * nt + col;
+      const int token = (at.first + r) / at.group;   // in its request
+      if (r >= at.count) {
+        bits = 0;
+      } else if (a.tree_mask) {
+        const uint64_t* words = a.tree_mask + (static_cast<int64_t>(at.start) + token) * a.mask_words;
+        const int w = idx < 0 ? 0 : idx >> 6;
+        uint64_t m = w < a.mask_words ? words[w] : 0;
+        if (idx < 0) {
+          m = (m << -idx) | ((uint64_t{1} << -idx) - 1);
+        } else {
+          const int sh = idx & 63;
+          m >>= sh;
+          if (sh > 32 && w + 1 < a.mask_words) m |= words[w + 1] << (64 - sh);
+        }
+        bits &= static_cast<uint32_t>(m);
+      } else {
+        const int vis = token - idx + 1;   // keys of the tile up to the token
+        bits &= vis >= 32 ? 0xFFFFFFFFu : vis <= 0 ? 0u : (1u << vis) - 1;
+      }
+    }
+    return bits;
+  };
   // Unseen keys score -infinity.
   if (DRAFTED || here != 0xFFFFFFFFu) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      uint32_t bits = here;
-      if constexpr (DRAFTED) {
-        const int r = 16 * nt + col;
-        const int token = (at.first + r) / at.group;   // in its request
-        if (r >= at.count) {
-          bits = 0;
-        } else if (a.tree_mask) {
-          const uint64_t* words = a.tree_mask + (static_cast<int64_t>(at.start) + token) * a.mask_words;
-          const int w = idx < 0 ? 0 : idx >> 6;
-          uint64_t m = w < a.mask_words ? words[w] : 0;
-          if (idx < 0) {
-            m = (m << -idx) | ((uint64_t{1} << -idx) - 1);
-          } else {
-            const int sh = idx & 63;
-            m >>= sh;
-            if (sh > 32 && w + 1 < a.mask_words) m |= words[w + 1] << (64 - sh);
-          }
-          bits &= static_cast<uint32_t>(m);
-        } else {
-          const int vis = token - idx + 1;   // keys of the tile up to the token
-          bits &= vis >= 32 ? 0xFFFFFFFFu : vis <= 0 ? 0u : (1u << vis) - 1;
-        }
-      }
+      const uint32_t bits = seen_by(nt);
 #pragma unroll
       for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
@@ -480,11 +485,13 @@ __device__ __forceinline__ void tile_step(const AttentionArgs& a, const Place& a
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       wait_lds_reads();
+      const uint32_t bits = seen_by(nt);   // a key that is seen may score -infinity, too
 #pragma unroll
       for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          ws[16 * (16 * kt + 4 * g + e) + col] = s[kt][nt][e] == -INFINITY ? static_cast<T>(-1.f) : w[nt][4 * kt + e];
+          ws[16 * (16 * kt + 4 * g + e) + col] =
+              bits >> (16 * kt + 4 * g + e) & 1 ? w[nt][4 * kt + e] : static_cast<T>(-1.f);
 #pragma unroll 1
       for (int k = 0; k < kTile; ++k) {
         const float x = static_cast<float>(ws[16 * k + col]);

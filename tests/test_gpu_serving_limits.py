@@ -231,3 +231,27 @@ def test_attention_scores_of_minus_infinity(heads, kvh, ctx, added, dtype):
     spread = np.full_like(spread, 64 * 12.0 * 6.0 * p.scale)
     lim = p.bound(out, weight, spread, keys)
     assert (np.abs(got - out)[first] <= lim[first]).all()
+
+
+@pytest.mark.parametrize("heads,kvh,ctx,added", ROWS)
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("drafted", [False, True])
+def test_attention_infinite_value_without_weight(heads, kvh, ctx, added, dtype, drafted):
+    """An infinite value whose key scores -infinity: 0 * infinity is NaN in its
+    channel for the rows that see it, and nothing for the others."""
+    p = Problem(ctx, added, heads, kvh, 64, 16, dtype, tree=True, seed=heads + 2)
+    say(f"infinite value without weight heads={heads}/{kvh} {dtype} drafted={drafted}")
+    p.q[:, :, 0] = 1.0
+    i = added[0] // 2
+    j = ctx[0] + i if drafted else 37
+    page, off = int(p.table[0, j // 16]), j % 16
+    p.kc[page, off, :, 0] = float("-inf")
+    p.vc[page, off, :, 5] = float("inf")
+    got = wide(p.run())
+    sees = np.zeros(p.T, dtype=bool)
+    for t in range(added[0]):
+        sees[t] = not drafted or bool((int(p.mask[t, 0]) >> i) & 1)
+    assert sees.any() and not sees.all()
+    assert np.isnan(got[sees][:, :, 5]).all()
+    assert np.isfinite(np.delete(got, 5, axis=2)).all()
+    assert np.isfinite(got[~sees]).all()
