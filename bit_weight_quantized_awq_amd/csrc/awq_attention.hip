@@ -244,12 +244,13 @@ __device__ __forceinline__ void load_rows(const AttentionArgs& a, const Place& a
   using T = typename Act<BF16>::T;
   const int lane = fresh(threadIdx.x & 63), col = lane & 15, g = lane >> 4;
   // A negative scale turns the queries' signs, so that the largest product is
-  // the largest score.  A zero scale becomes one that leaves every finite
-  // score at zero.
+  // the largest score.  A zero scale, which would make NaN of a hidden key's
+  // -infinity, becomes the smallest one: it leaves every finite product, of
+  // 2^128 at most, within 2^-21 of zero.
   float c = a.scale * 1.44269504088896340736f;
   if (a.cache.k_scale) c *= static_cast<const float*>(a.cache.k_scale)[hk];
   const uint32_t flip = c < 0.f ? 0x80008000u : 0u;
-  o.c = fmaxf(fabsf(c), 1e-37f);
+  o.c = fmaxf(fabsf(c), 0x1p-149f);
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int r = at.first + 16 * nt + col;

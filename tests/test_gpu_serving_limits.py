@@ -255,3 +255,31 @@ def test_attention_infinite_value_without_weight(heads, kvh, ctx, added, dtype, 
     assert np.isnan(got[sees][:, :, 5]).all()
     assert np.isfinite(np.delete(got, 5, axis=2)).all()
     assert np.isfinite(got[~sees]).all()
+
+
+@pytest.mark.parametrize("heads,kvh,ctx,added", ROWS)
+@pytest.mark.parametrize("scale,size", [(0.0, 1e18), (1e-38, 4e18), (-3e-38, 4e18), (1e-41, 1e18),
+                                        (1e-60, 1e18)])
+def test_attention_smallest_scales(heads, kvh, ctx, added, scale, size):
+    """Scales at and near zero over bfloat16 products of up to 1e38.
+
+    Errors: as Problem.bound; a scale below 2^-126 is a multiple of 2^-149, so
+    scores move by half of that times the product, at most 2^-150 * 64 *
+    size^2, and a zero scale counts as 2^-149."""
+    p = Problem(ctx, added, heads, kvh, 64, 16, BF16, tree=True, seed=heads + 3)
+    say(f"scale {scale} products of {size * size}")
+    p.kc.mul_(size)
+    p.q.copy_(torch.nan_to_num(p.q * (size / 8)))
+    p.scale = scale
+    got = wide(p.run(scale=scale))
+    out, weight, spread, keys = p.want()
+    small = 0.0
+    if abs(scale) < 2.0 ** -126:
+        top = np.nanmax(np.abs(wide(p.kc))) * np.abs(wide(p.q)).max() * 64
+        small = 2.0 ** -148 * 1.45 * top
+        assert small < 1e-4
+    assert np.isfinite(got).all()
+    lim = p.bound(out, weight, spread, keys) + 2 * small * weight
+    assert (np.abs(got - out) <= lim).all(), np.abs(got - out).max()
+    if scale != 0 and abs(scale) > 1e-40:
+        assert np.abs(out - wide(p.run(scale=0.0))).max() > 0.1   # the scale matters
