@@ -42,3 +42,12 @@ def test_layout_kernel_where_sums_pass_32_bits(tmp_path):
     out = run_checked(tmp_path, "layout_check", [os.path.join(NATIVE, "layout_check.cpp")],
                       [str(tmp_path), NATIVE, CSRC, os.path.join(ROOT, "include")])
     assert "layout_check ok" in out
+
+
+def test_validation_and_planning(tmp_path):
+    """The checks of arguments, and what a plan writes against the workspace
+    it asks for, over extreme sizes."""
+    out = run_checked(tmp_path, "verify_check",
+                      [os.path.join(NATIVE, "verify_check.cpp"), os.path.join(CSRC, "awq_verify.cpp"),
+                       os.path.join(CSRC, "awq_plan.cpp")], [CSRC, os.path.join(ROOT, "include")])
+    assert "verify_check ok" in out
