@@ -1,6 +1,8 @@
 // Host-side validation of the serving-pass operators (HIP-free).
 #include "awq_verify.h"
 
+#include <float.h>
+
 #include "awq_plan.h"
 
 namespace awq {
@@ -86,7 +88,7 @@ int validate_attention(const AttentionArgs& a, const awq_kv_cache* cache, int64_
   if (B <= 0 || T < 0 || heads <= 0 || table_width <= 0 || mask_words < 0 || a.table_stride < 0 ||
       a.q_token_stride < 0 || a.q_head_stride < 0 || !activation_dtype(a.dtype))
     return AWQ_ERROR_INVALID_VALUE;
-  if (!(scale - scale == 0.0)) return AWQ_ERROR_INVALID_VALUE;  // infinite or NaN
+  if (!(scale >= -FLT_MAX && scale <= FLT_MAX)) return AWQ_ERROR_INVALID_VALUE;
   const int st = validate_cache(cache);
   if (st != AWQ_SUCCESS) return st;
   if (cache->dtype != AWQ_E4M3 && cache->dtype != a.dtype) return AWQ_ERROR_INVALID_VALUE;

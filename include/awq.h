@@ -422,7 +422,8 @@ int awq_kv_write(const void* k, const void* v, const void* slots, const awq_kv_c
  * dtype or AWQ_E4M3 (its elements are exact in either).  block_table (B,
  * table_width) with row stride table_stride; tree_mask int64 (T, mask_words)
  * or NULL.  head_dim is 64, 128 or 256 and heads a multiple of the cache's,
- * else AWQ_ERROR_SHAPE.  Scores, softmax statistics and sums are float32;
+ * else AWQ_ERROR_SHAPE.  scale is finite as a float32, else
+ * AWQ_ERROR_INVALID_VALUE.  Scores, softmax statistics and sums are float32;
  * the softmax weights are rounded to dtype before they multiply v.
  *
  * workspace: awq_tree_attention_workspace_size(...) bytes, 256-byte

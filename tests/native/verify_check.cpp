@@ -175,7 +175,8 @@ static void check_attention() {
   const awq_kv_cache c = cache(10, 16, 8, 128, AWQ_F16);
   const auto scaled = [&](double scale) { return validate_attention(a, &c, 2, 4, 32, 8, 0, scale); };
   for (double s : {0.0, -1.0, 1e-300, 1e38, -static_cast<double>(FLT_MAX)}) EXPECT(scaled(s) == AWQ_SUCCESS);
-  for (double s : {static_cast<double>(INFINITY), static_cast<double>(NAN)})
+  // What float32 does not hold would make every score infinite.
+  for (double s : {1e39, -1e300, static_cast<double>(INFINITY), static_cast<double>(NAN)})
     EXPECT(scaled(s) == AWQ_ERROR_INVALID_VALUE);
 }
 
