@@ -6,8 +6,8 @@ loads it from.  Packed fp32 VALU instructions are disabled in device code.
 A second, separate library, libawq_bench.so (csrc/bench_read.hip: a plain
 read stream that the benchmark uses as a same-box reference), is built the
 same way; the W4A16 path never loads it.  _serving.so (csrc/serving_bind.cpp,
-host code against torch's headers) is the Python module behind serving.py; it
-links the library.
+host code against torch's headers, left out where torch is missing) is the
+Python module behind serving.py; it links the library.
 """
 from __future__ import annotations
 
@@ -90,16 +90,25 @@ def _compile(src: str, extra: list[str]) -> str:
 
 
 def build(verbose: bool = False, extra_flags: list[str] | None = None, jobs: int = 6) -> str:
-    """Compile every HIP source for gfx950 and link the shared library.
-    Always recompiles.  Returns the library path."""
+    """Compile every HIP source for gfx950 and link the shared library, and
+    where torch can be imported its Python module.  Always recompiles.
+    Returns the library path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     extra = list(extra_flags or [])
+    try:
+        import torch  # noqa: F401
+        with_torch = True
+    except ImportError:
+        with_torch = False
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
-        bind = ex.submit(_compile_bind)
+        bind = ex.submit(_compile_bind) if with_torch else None
         objs = list(ex.map(lambda s: _compile(s, extra), SOURCES + BENCH_SOURCES))
     _link(objs[:len(SOURCES)], LIB_PATH, verbose)
     _link(objs[len(SOURCES):], BENCH_LIB_PATH, verbose)
-    _link_bind(bind.result(), verbose)
+    if bind:
+        _link_bind(bind.result(), verbose)
+    elif verbose:
+        print(f"{os.path.basename(BIND_PATH)} is left out: torch cannot be imported")
     return LIB_PATH
 
 
@@ -109,6 +118,12 @@ def _run(cmd: list[str], what: str) -> None:
         raise RuntimeError(f"{what} failed:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
 
 
+def _host_compiler(*language: str) -> list[str]:
+    """g++, or the compiler that builds the library (given the language)."""
+    gxx = shutil.which("g++")
+    return [gxx] if gxx else [hipcc(), *language]
+
+
 def _compile_bind() -> str:
     import sysconfig
 
@@ -116,11 +131,11 @@ def _compile_bind() -> str:
     from torch.utils import cpp_extension
     obj = os.path.join(BUILD_DIR, BIND_SOURCE + ".o")
     includes = [sysconfig.get_paths()["include"]] + cpp_extension.include_paths("cuda")
-    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall",
+    _run(_host_compiler("-x", "c++") + ["-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall",
           "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{INCLUDE}"] +
          [x for i in includes for x in ("-isystem", i)] +
-         ["-c", os.path.join(CSRC, BIND_SOURCE), "-o", obj], f"g++ for {BIND_SOURCE}")
+         ["-c", os.path.join(CSRC, BIND_SOURCE), "-o", obj], f"compiling {BIND_SOURCE}")
     return obj
 
 
@@ -129,7 +144,7 @@ def _link_bind(obj: str, verbose: bool) -> None:
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = BIND_PATH + ".tmp"
     # torch has loaded its own libraries before it imports this one.
-    _run(["g++", "-shared", "-o", tmp, obj, f"-L{libs}", "-lc10", "-lc10_hip", "-ltorch_cpu",
+    _run(_host_compiler() + ["-shared", "-o", tmp, obj, f"-L{libs}", "-lc10", "-lc10_hip", "-ltorch_cpu",
           "-ltorch_python", f"-L{PKG_DIR}", f"-l:{LIB_NAME}", "-Wl,-rpath,$ORIGIN"],
          "linking _serving.so")
     os.replace(tmp, BIND_PATH)
