@@ -283,3 +283,101 @@ def test_attention_smallest_scales(heads, kvh, ctx, added, scale, size):
     assert (np.abs(got - out) <= lim).all(), np.abs(got - out).max()
     if scale != 0 and abs(scale) > 1e-40:
         assert np.abs(out - wide(p.run(scale=0.0))).max() > 0.1   # the scale matters
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("bs,tree", [(16, True), (24, True), (64, False)])
+def test_attention_32_rows_over_long_contexts(D, dtype, e4m3, bs, tree):
+    """17 to 32 rows of a key head on average: waves go over many tiles, and
+    row blocks are split over work-groups and joined."""
+    added = [5, 6, 7, 5]
+    assert 16 < sum(added) * 4 / len(added) <= 32
+    Problem([4100, 37, 1900, 6], added, 8, 2, D, bs, dtype, e4m3, tree=tree, seed=D + bs).check(
+        f"32 rows D={D} {dtype} e4m3={e4m3} bs={bs} tree={tree}")
+
+
+class Sampled:
+    """A long problem whose rows are checked for some of its heads only.
+    Errors are bounded as in Problem.bound."""
+
+    def __init__(self, ctx, added, heads, D, bs, dtype, e4m3, seed):
+        gen = torch.Generator(DEV).manual_seed(seed)
+        self.dtype, self.ctx, self.added, self.D, self.bs = dtype, ctx, added, D, bs
+        used = [-(-(c + n) // bs) for c, n in zip(ctx, added)]
+        blocks = sum(used) + 3
+        ids = np.random.default_rng(seed).permutation(blocks)
+        self.table = np.full((len(ctx), max(used)), -1, dtype=np.int32)
+        at = 0
+        for b, u in enumerate(used):
+            self.table[b, :u] = ids[at:at + u]
+            at += u
+
+        def rand(*shape):
+            return torch.randn(shape, generator=gen, device=DEV, dtype=torch.float16)
+
+        self.kc, self.vc = (rand(blocks, bs, heads, D).to(E4M3 if e4m3 else dtype) for _ in range(2))
+        self.q = rand(sum(added), heads, D).to(dtype)
+        self.q_start = np.concatenate([[0], np.cumsum(added)]).astype(np.int32)
+        self.heads = heads
+
+    def check(self, what, sample):
+        from oracle import serving_oracle as ref
+        say(what)
+        got = wide(awq.tree_attention(self.q, self.kc, self.vc, i32(self.table), i32(self.ctx),
+                                      i32(self.q_start)))[:, sample]
+        assert np.isfinite(got).all()
+        part = Problem.__new__(Problem)
+        part.D, part.dtype, part.v_scale = self.D, self.dtype, None
+        part.vc = self.vc[:, :, sample]
+        out, weight, spread, keys = ref.tree_attention(
+            wide(self.q[:, sample]), wide(self.kc[:, :, sample]), wide(part.vc), self.table, self.ctx,
+            self.q_start, None, self.D ** -0.5)
+        lim = part.bound(out, weight, spread, keys)
+        bad = np.abs(got - out) > lim
+        assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:4].tolist())
+
+
+@pytest.mark.parametrize("D,dtype,e4m3,bs", [
+    (64, F16, False, 16), (64, BF16, False, 16), (128, F16, True, 16), (64, F16, True, 32),
+    (64, F16, False, 24), (128, BF16, True, 20), (256, F16, False, 8)])
+def test_attention_runs_of_many_steps(D, dtype, e4m3, bs):
+    """As many key heads as work-groups and more than 32 rows of each, so one
+    work-group goes over a whole context: more steps than pages are looked up
+    for at once (64 steps of 64 or 128 keys), with pages that hold whole
+    groups of keys and pages that do not."""
+    heads = 256
+    step = 128 if D == 64 and e4m3 else 64
+    ctx = [64 * step * 2 + 300, 50]
+    Sampled(ctx, [35, 34], heads, D, bs, dtype, e4m3, seed=D + bs).check(
+        f"many steps D={D} {dtype} e4m3={e4m3} bs={bs}", [0, 7, 255])
+
+
+def test_layout_trees_of_many_requests():
+    """More requests than threads keep in registers (four of 256 threads), with
+    trees, masks of two words and a capacity that cuts the last ones."""
+    from oracle import serving_oracle as ref
+    from test_gpu_serving import random_parents
+    say("batch_layout trees of 1500 requests")
+    B = 1500
+    rng = np.random.default_rng(1)
+    cached, added = rng.integers(0, 200, B), rng.integers(0, 9, B)
+    added[[3, 700, 1499]] = [90, 1, 130]
+    held = -(-cached // 16)
+    table = np.full((B, 24), -1, dtype=np.int32)
+    ids = rng.permutation(40000).astype(np.int32)
+    at = 0
+    for b in range(B):
+        table[b, :held[b]] = ids[at:at + held[b]]
+        at += held[b]
+    free = ids[at:at + 1200]
+    T = int(added.sum()) - 7
+    parents = random_parents(rng, added)[:T]
+    want = ref.batch_layout(cached, added, held, free, 5, table, 16, 40000, T, parents, 2)
+    t = i32(table)
+    got = awq.batch_layout(i32(cached), i32(added), i32(held), i32(free), t, 16, 40000, T,
+                           parents=i32(parents), mask_words=2, free_start=i32([5]))
+    np.testing.assert_array_equal(num(t), want["block_table"])
+    for key in ("q_start", "slots", "positions", "requests", "blocks_held", "status", "tree_mask"):
+        np.testing.assert_array_equal(num(getattr(got, key)), want[key], err_msg=key)
