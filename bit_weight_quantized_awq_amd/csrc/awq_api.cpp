@@ -20,13 +20,19 @@ const char* awq_status_string(int status) {
   switch (status) {
     case AWQ_SUCCESS: return "success";
     case AWQ_ERROR_INVALID_VALUE:
-      return "invalid value (NULL pointer, negative or zero size, bad group_size, "
+      return "invalid value (NULL pointer, negative or zero size, bad group_size or dtype, "
+             "a scale that is not finite in float32, "
              "or a kernel path that cannot run this problem)";
     case AWQ_ERROR_SHAPE:
       return "shape error (out_features % 8 != 0, in_features % group_size != 0, "
+             "a head_dim or number of heads that the call has no kernel for, "
              "or an operand with 2^31 or more elements)";
-    case AWQ_ERROR_MISALIGNED: return "pointer not aligned to its element size";
-    case AWQ_ERROR_WORKSPACE: return "workspace missing or smaller than awq_gemm_workspace_size";
+    case AWQ_ERROR_MISALIGNED:
+      return "pointer not aligned to its element size (queries, keys, values, caches and their "
+             "strides: to 16 bytes)";
+    case AWQ_ERROR_WORKSPACE:
+      return "workspace missing or smaller than awq_gemm_workspace_size "
+             "(awq_gemm_sorted_workspace_size, awq_tree_attention_workspace_size)";
     case AWQ_ERROR_HIP: return "HIP launch error";
     case AWQ_ERROR_SCRATCH:
       return "problem needs more split-K workspace than awq_gemm_noalloc's fixed scratch "

@@ -56,11 +56,14 @@ extern "C" {
 enum awq_status {
   AWQ_SUCCESS = 0,
   AWQ_ERROR_INVALID_VALUE = 1, /* NULL required pointer, M < 0, K <= 0, N <= 0,
-                                  group_size == 0 or < -1, unknown path request */
+                                  group_size == 0 or < -1, unknown path request,
+                                  a dtype or scale that the call does not take */
   AWQ_ERROR_SHAPE = 2,         /* N % 8 != 0, K % group_size != 0 (page checks),
+                                  heads or a head_dim without a kernel,
                                   or an operand with 2^31 or more elements */
-  AWQ_ERROR_MISALIGNED = 3,    /* a pointer not aligned to its element size */
-  AWQ_ERROR_WORKSPACE = 4,     /* workspace smaller than awq_gemm_workspace_size */
+  AWQ_ERROR_MISALIGNED = 3,    /* a pointer not aligned to its element size, or
+                                  to 16 bytes where an entry point says so */
+  AWQ_ERROR_WORKSPACE = 4,     /* workspace smaller than the call's size function says */
   AWQ_ERROR_HIP = 5,           /* a HIP launch reported an error */
   AWQ_ERROR_SCRATCH = 6        /* awq_gemm_noalloc: the problem's split-K workspace
                                   exceeds AWQ_NOALLOC_SCRATCH_BYTES */

@@ -212,3 +212,30 @@ def test_masks_of_no_words_are_refused(stub):
         assert stub.stub_launches() == 0
         print("ok")
         """))
+
+
+def test_refusals_say_what_serving_calls_refuse(stub):
+    """The texts of the statuses name the limits of these calls, too."""
+    run(stub, DEVICES + textwrap.dedent("""
+        import re
+        q, cache = new(4, 8, 96, dtype=F16), new(10, 16, 2, 96, dtype=F16)
+        small = new(16, dtype=torch.uint8)
+        good, fine = new(4, 8, 64, dtype=F16), new(10, 16, 2, 64, dtype=F16)
+        shifted = torch.empty(4 * 8 * 64 + 1, dtype=F16, device="cuda:1")[1:].view(4, 8, 64)
+        for call, words in [
+                (lambda: awq.tree_attention(q, cache, cache, new(2, 4), new(2), new(3), workspace=small),
+                 "head_dim"),
+                (lambda: awq.tree_attention(good, fine, fine, new(2, 4), new(2), new(3), workspace=small),
+                 "awq_tree_attention_workspace_size"),
+                (lambda: awq.tree_attention(shifted, fine, fine, new(2, 4), new(2), new(3),
+                                            workspace=small), "16 bytes"),
+                (lambda: awq.tree_attention(good, fine, fine, new(2, 4), new(2), new(3), scale=1e39,
+                                            workspace=small), "finite")]:
+            try:
+                call()
+            except awq.AwqError as e:
+                assert words in str(e), (words, str(e))
+            else:
+                raise AssertionError("no exception")
+        print("ok")
+        """))
