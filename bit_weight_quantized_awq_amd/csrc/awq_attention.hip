@@ -42,7 +42,13 @@
 //   over lanes and no rescaling of the sums.  A row's largest weight lies in
 //   2^7 .. 2^15: the top of float16's range, so the weights that are rounded
 //   to it for the matrix cores keep their precision down to 2^-21 of the
-//   largest, and a long context of small ones is not lost.
+//   largest, and a long context of small ones is not lost.  Their sum is of
+//   the unrounded ones.  The rounding to 16 bits takes the error against 64
+//   bits from that of the rounded output alone, 2.1e-4 of its size in float16
+//   and 1.7e-3 in bfloat16, to 2.8e-4 and 2.2e-3; a second product with what
+//   it leaves over takes it back, but 131K context then takes 158.7 us and
+//   not 134.0, trees of 13-64 tokens 81.8 and not 74.2, e4m3 trees 211 and
+//   not 206.
 #include <float.h>
 #include <math.h>
 

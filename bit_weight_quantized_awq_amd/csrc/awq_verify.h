@@ -12,7 +12,8 @@ namespace awq {
 
 constexpr int64_t kInt32Max = (int64_t{1} << 31) - 1;
 
-// awq_batch_layout keeps two int32 prefix sums per request in LDS.
+// awq_batch_layout keeps two int32 prefix sums per request in LDS, and up to
+// 1024 requests two of their lengths as well.
 constexpr int64_t kLayoutMaxRequests = 16384;
 
 // awq_process_logits packs, per vocabulary entry, the count of the output

@@ -3,8 +3,8 @@
 // in one function each.  A pass makes these calls once a layer, and at small
 // batches the host's time is what they cost: checked and marshalled in Python
 // through ctypes they took 8.4-14.6 us each, more than their kernels; here
-// kv_write takes 3.8, process_logits 4.7, batch_layout 5.8 and tree_attention
-// 7.6 us, launches included.  Only host code: the compute is behind
+// kv_write takes 3.3, process_logits 4.5, batch_layout 5.4 and tree_attention
+// 6.8 us, launches included.  Only host code: the compute is behind
 // include/awq.h.
 #include <torch/csrc/python_headers.h>
 

@@ -413,8 +413,9 @@ int awq_kv_write(const void* k, const void* v, const void* slots, const awq_kv_c
  *   seen  = j < cached_lens[b], or bit j - cached_lens[b] of tree_mask[t]
  *           (without tree_mask: j - cached_lens[b] <= i, a causal chain)
  *   out[t, h] = sum over seen j of softmax(s)_j v_j
- * A row that sees nothing is 0; an unseen key or value changes nothing,
- * whatever it holds (infinities and NaN too).  Cache indices whose block is
+ * A row that sees nothing is 0 (one whose scores are all -infinity is NaN);
+ * an unseen key or value changes nothing, whatever it holds (infinities and
+ * NaN too).  Cache indices whose block is
  * outside [0, num_blocks) or past table_width count as unseen.  Rows of q
  * outside every request get 0.  A negative length counts as 0, and q_start
  * is clipped to [0, T].
